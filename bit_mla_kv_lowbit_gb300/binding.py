@@ -53,11 +53,37 @@ class Layout(ctypes.Structure):
 
 
 def layout(content_bits: int = 4, rope_bits: int = 4, rotate: bool = False) -> Layout:
-    return Layout(content_bits, rope_bits, 64, 4, 128, 64, 512, 64, int(bool(rotate)))
+    return Layout(_int32(content_bits, "content_bits"), _int32(rope_bits, "rope_bits"), 64, 4, 128, 64, 512, 64,
+                  int(bool(rotate)))
 
 
 class LibraryError(RuntimeError):
     pass
+
+
+# The ABI's ints hold 32 bits, and ctypes keeps the low 32 of a larger number
+# without an error: what does not fit is refused here.
+_INT32_MAX = 2 ** 31 - 1
+_ESIZE = -4
+
+
+def _int32(v, name: str) -> int:
+    v = int(v)
+    if not -_INT32_MAX - 1 <= v <= _INT32_MAX:
+        raise ValueError(f"{name} must fit in 32 bits, got {v}")
+    return v
+
+
+def _tokens(v) -> int:
+    """A window or a number of first tokens: they may exceed every sequence, and
+    no sequence is longer than an int32, so what is beyond that is all tokens (and
+    below 0 out of range)."""
+    return min(max(int(v), -1), _INT32_MAX)
+
+
+def _check_sizes(what: str, *sizes: int):
+    if max(sizes) > _INT32_MAX:
+        _check(_ESIZE, what)
 
 
 def lib_path() -> str:
@@ -155,8 +181,8 @@ def decode_plan(lay: Layout, heads: int, seq_lens_host: Sequence[int], num_sms: 
     """Returns ``(total_splits, chunk_pages, workspace_bytes)``."""
     lens = np.ascontiguousarray(np.asarray(seq_lens_host, dtype=np.int32))
     tot, chunk, ws = ctypes.c_int(), ctypes.c_int(), ctypes.c_size_t()
-    st = load().mla_lowbit_decode_plan(ctypes.byref(lay), len(lens), int(heads),
-                                       lens.ctypes.data_as(ctypes.c_void_p), int(num_sms),
+    st = load().mla_lowbit_decode_plan(ctypes.byref(lay), len(lens), _int32(heads, "heads"),
+                                       lens.ctypes.data_as(ctypes.c_void_p), _int32(num_sms, "num_sms"),
                                        ctypes.byref(tot), ctypes.byref(chunk), ctypes.byref(ws))
     _check(st, "mla_lowbit_decode_plan")
     return tot.value, chunk.value, ws.value
@@ -223,6 +249,7 @@ def write(lay: Layout, ckv, krope, pos, block_table, page_pool, sink_buf, recent
     _expect(page_pool, "page_pool", torch.uint8)
     _expect(err_word, "err_word", torch.int32, (1,))
     num_seqs, max_pages = block_table.shape
+    _check_sizes("mla_lowbit_write", n, num_seqs, max_pages)
     if seq_idx is not None:
         _expect(seq_idx, "seq_idx", torch.int32, (n,))
     if seq_lens_after is not None:
@@ -260,6 +287,7 @@ def decode(lay: Layout, q, page_pool, block_table, seq_lens, seq_lens_host, sink
         _expect(lse, "lse", torch.float32, (B, H))
     if block_table.shape[0] != B:
         raise ValueError("block_table must have one row per sequence")
+    _check_sizes("mla_lowbit_decode", B, H, block_table.shape[1])
     if lay.content_bits != 16:
         _expect(sink_buf, "sink_buf", torch.bfloat16, (B, 4, 576))
         _expect(recent_buf, "recent_buf", torch.bfloat16, (B, 128, 576))
@@ -297,6 +325,7 @@ def write_decode(lay: Layout, q, ckv_new, krope_new, page_pool, block_table, seq
         _expect(lse, "lse", torch.float32, (B, H))
     if block_table.shape[0] != B:
         raise ValueError("block_table must have one row per sequence")
+    _check_sizes("mla_lowbit_write_decode", B, H, block_table.shape[1])
     if lay.content_bits != 16:
         _expect(sink_buf, "sink_buf", torch.bfloat16, (B, 4, 576))
         _expect(recent_buf, "recent_buf", torch.bfloat16, (B, 128, 576))
@@ -333,6 +362,7 @@ def decode_multi(lay: Layout, q, page_pool, block_table, seq_lens, seq_lens_host
         _expect(lse, "lse", torch.float32, (B, n, H))
     if block_table.shape[0] != B:
         raise ValueError("block_table must have one row per sequence")
+    _check_sizes("mla_lowbit_decode_multi", B, H, block_table.shape[1])
     if lay.content_bits != 16:
         _expect(sink_buf, "sink_buf", torch.bfloat16, (B, 4, 576))
         _expect(recent_buf, "recent_buf", torch.bfloat16, (B, 128, 576))
@@ -370,6 +400,7 @@ def decode_noalloc(lay: Layout, q, page_pool, block_table, seq_lens, seq_lens_ho
         _expect(lse, "lse", torch.float32, (B, H))
     if block_table.shape[0] != B:
         raise ValueError("block_table must have one row per sequence")
+    _check_sizes("mla_lowbit_decode_noalloc", B, H, block_table.shape[1])
     if lay.content_bits != 16:
         _expect(sink_buf, "sink_buf", torch.bfloat16, (B, 4, 576))
         _expect(recent_buf, "recent_buf", torch.bfloat16, (B, 128, 576))
@@ -434,6 +465,9 @@ def _native(name, *args):
 def _launch(call, what, index, args, stream):
     """Calls the library with the current device set to CUDA device ``index``."""
     torch = _torch()
+    for v, kind in zip(args, call.argtypes):
+        if kind is ctypes.c_int and not -_INT32_MAX - 1 <= v <= _INT32_MAX:
+            _check(_ESIZE, what)
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == index:
         st = call(*args, s)
@@ -536,10 +570,11 @@ def rope_table(dim: int, theta: float = 10000.0, scaling: str = "none", factor: 
     pair's turn per position in 2^-64 turns) and the factor on rotated values."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {ROPE_SCALINGS}, got {scaling!r}")
-    phase = np.zeros(max(int(dim) // 2, 1), np.uint64)
+    dim = _int32(dim, "dim")
+    phase = np.zeros(max(dim // 2, 1), np.uint64)
     mscale = ctypes.c_float()
-    _check(load().mla_lowbit_rope_table(int(dim), float(theta), ROPE_SCALINGS.index(scaling), float(factor),
-                                        int(original_len), float(beta_fast), float(beta_slow),
+    _check(load().mla_lowbit_rope_table(dim, float(theta), ROPE_SCALINGS.index(scaling), float(factor),
+                                        _int32(original_len, "original_len"), float(beta_fast), float(beta_slow),
                                         phase.ctypes.data_as(ctypes.c_void_p), ctypes.byref(mscale)),
            "mla_lowbit_rope_table")
     return phase, mscale.value
@@ -696,9 +731,10 @@ def window_plan(lay: Layout, num_seqs: int, heads: int, queries: int, window: in
     """``(splits_per_seq, workspace_bytes)`` of decode_window, for every step of
     a cache of these sizes, whatever its lengths."""
     splits, nbytes = ctypes.c_int(), ctypes.c_size_t()
-    _check(load().mla_lowbit_window_plan(ctypes.byref(lay), int(num_seqs), int(heads), int(queries), int(window),
-                                         int(sinks), int(max_pages), int(num_sms), ctypes.byref(splits),
-                                         ctypes.byref(nbytes)), "mla_lowbit_window_plan")
+    _check(load().mla_lowbit_window_plan(
+        ctypes.byref(lay), _int32(num_seqs, "num_seqs"), _int32(heads, "heads"), _int32(queries, "queries"),
+        _tokens(window), _tokens(sinks), _int32(max_pages, "max_pages"), _int32(num_sms, "num_sms"),
+        ctypes.byref(splits), ctypes.byref(nbytes)), "mla_lowbit_window_plan")
     return splits.value, nbytes.value
 
 
@@ -730,8 +766,8 @@ def decode_window(lay: Layout, q, page_pool, block_table, seq_lens, sink_buf, re
         (out, "out", out.dtype, lead + (512,)), (lse, "lse", f32, [lead]), (workspace, "workspace", u8, None),
         (err_word, "err_word", i32, (1,))))
     _launch(load().mla_lowbit_decode_window, "mla_lowbit_decode_window", index,
-            (ctypes.byref(lay), S, lead[1] if len(lead) == 3 else 1, lead[-1], softmax_scale, int(window), int(sinks), qp, pool,
-             num_pages, table, max_pages, lens, sink, recent, code, o, ls, ws, workspace.numel(), err), stream)
+            (ctypes.byref(lay), S, lead[1] if len(lead) == 3 else 1, lead[-1], softmax_scale, _tokens(window), _tokens(sinks), qp,
+             pool, num_pages, table, max_pages, lens, sink, recent, code, o, ls, ws, workspace.numel(), err), stream)
     return out
 
 
@@ -739,7 +775,7 @@ def set_fault_injection(mode: int, wait_cycles: int = 0) -> None:
     """Self-test setting of the tcgen05 kernels' bounded waits (process-wide):
     mode 1 withholds one hand-off so that the waits run out after
     ``wait_cycles`` SM cycles (0 = the default limit); mode 0 is normal."""
-    _check(load().mla_lowbit_set_fault_injection(int(mode), int(wait_cycles)),
+    _check(load().mla_lowbit_set_fault_injection(_int32(mode, "mode"), min(max(int(wait_cycles), -1), 2 ** 63 - 1)),
            "mla_lowbit_set_fault_injection")
 
 

@@ -73,7 +73,7 @@ struct Args {
     if (fine && ((v == -1 && PyErr_Occurred()) || v < INT32_MIN || v > INT32_MAX)) refuse();
     return (int)v;
   }
-  // (sizes that an int cannot hold: the Python path has the library refuse them)
+  // (sizes that an int cannot hold are refused by the Python path)
   int size(int64_t v) {
     if (v > INT32_MAX) fine = false;
     return (int)v;
