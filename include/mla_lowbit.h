@@ -238,6 +238,8 @@ int mla_lowbit_write_decode(const mla_lowbit_layout* layout, int num_seqs, int h
  * 0 .. L - n + i.  Same arithmetic, tolerance and errors as mla_lowbit_decode
  * otherwise; the n queries run as n blocks of `heads` rows over one pass of the
  * cache (the masked tokens are all inside the recent window, 1 <= n <= 16).
+ * On the 128-row kernel a value of these n tokens that is not finite reaches all
+ * queries that share its 128 rows, also those before it.
  *
  *   q      [num_seqs][n][heads][576] bf16
  *   out    [num_seqs][n][heads][512] float32; lse [num_seqs][n][heads] or NULL
@@ -425,7 +427,8 @@ int mla_lowbit_window_plan(const mla_lowbit_layout* layout, int num_seqs, int he
  * may exceed the sequence (window >= its length: plain causal attention).  A
  * query with p < 0 (a sequence of fewer than n tokens, 0 for an idle row of the
  * batch) sees nothing: its output is 0 and its lse -inf.  The pages of tokens
- * that no query sees are not touched, and their block_table entries not read.
+ * that no query sees are not touched, and their block_table entries not read; a
+ * token whose values are not finite reaches the queries that see it and no other.
  * seq_lens is read on the device only.
  *   q    [num_seqs][n][heads][576] bf16
  *   out  [num_seqs][n][heads][512] float32 or bf16 (out_dtype)
