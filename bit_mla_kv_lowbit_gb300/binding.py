@@ -43,6 +43,7 @@ EXPORTS = (
 
 DEV_BAD_SEQ, DEV_BAD_POS, DEV_BAD_PAGE, DEV_BAD_LEN, DEV_PLAN, DEV_PIPELINE = 1, 2, 4, 8, 16, 32
 DEV_NO_ROOM = 64
+_CLEAR_SKIPPED = 0x100  # MLA_LOWBIT_CLEAR_SKIPPED
 ROPE_SCALINGS = ("none", "linear", "ntk", "yarn")  # the ABI's MLA_LOWBIT_ROPE_* values, in order
 
 
@@ -702,15 +703,19 @@ def _value_type(out):
 
 
 def read(lay: Layout, seq_idx, pos, block_table, page_pool, sink_buf, recent_buf, out, err_word, *, seq_lens=None,
-         stream=None):
+         clear_skipped: bool = False, stream=None):
     """The cached tokens (seq_idx[i], pos[i]) as values, out [n][576] bf16 or
     float32 (mla_lowbit_read).  With ``seq_lens`` protected tokens come from the
-    bf16 buffers, as decode sees them; without, every token's packed copy."""
-    if _native("read", lay, seq_idx, pos, block_table, page_pool, sink_buf, recent_buf, out, err_word, seq_lens, stream):
+    bf16 buffers, as decode sees them; without, every token's packed copy.  The
+    rows of padding and of tokens with an error stay as they were, or
+    (``clear_skipped``) become zeros."""
+    clear_skipped = bool(clear_skipped)
+    if _native("read", lay, seq_idx, pos, block_table, page_pool, sink_buf, recent_buf, out, err_word, seq_lens,
+               clear_skipped, stream):
         return out
     torch = _torch()
     index, S, max_pages, num_pages = _expect_pool(lay, block_table, page_pool)
-    code = _value_type(out)
+    code = _value_type(out) | (_CLEAR_SKIPPED if clear_skipped else 0)
     if pos is None:
         raise ValueError("pos is required")
     n, bf, i32 = pos.numel(), torch.bfloat16, torch.int32

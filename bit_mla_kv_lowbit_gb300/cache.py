@@ -90,11 +90,13 @@ class PagedCache:
     def read(self, seq_idx, pos, seq_lens=None, out=None, stream=None):
         """Cached tokens as values, [n][576] (bf16 unless ``out`` is float32):
         as decode sees them in sequences of ``seq_lens``, or (None) their packed
-        copies."""
-        if out is None:
+        copies.  The rows of padding (``seq_idx < 0``) and of tokens with an error
+        are zeros, or in a given ``out`` stay as they were."""
+        new = out is None
+        if new:
             out = binding.new_output((pos.shape[0], 576), self.torch.bfloat16, self.device, stream)
         return binding.read(self.layout, seq_idx, pos, self.block_table, self.pool, self.sink, self.recent,
-                            out, self.err, seq_lens=seq_lens, stream=stream)
+                            out, self.err, seq_lens=seq_lens, clear_skipped=new, stream=stream)
 
     def decode_window(self, q, seq_lens, softmax_scale: float, window: int, sinks: int = 0, out=None,
                       lse=None, workspace=None, stream=None):

@@ -280,7 +280,7 @@ PyObject* norm_rope_write(PyObject* const* v) {
   });
 }
 
-// layout, seq_idx, pos, block_table, page_pool, sink_buf, recent_buf, out, err_word, seq_lens, stream
+// layout, seq_idx, pos, block_table, page_pool, sink_buf, recent_buf, out, err_word, seq_lens, clear_skipped, stream
 PyObject* read(PyObject* const* v) {
   Args a;
   const Layout lay(a, v[0]);
@@ -294,11 +294,12 @@ PyObject* read(PyObject* const* v) {
   const Buffers buf(a, lens && lay.packed(), c.seqs, v[5], v[6]);
   void* out = a.ptr(v[7], scalar(code), {n, 576});
   int32_t* err = a.ints<int32_t>(v[8], {1});
-  void* stream = a.stream(v[10]);
+  const int clear = a.integer(v[10]) ? MLA_LOWBIT_CLEAR_SKIPPED : 0;
+  void* stream = a.stream(v[11]);
   if (!a.fine) return nullptr;
   return launched([&] {
-    return lib.read(lay.l, n, idx, pos, c.seqs, lens, c.table, c.max_pages, c.pool, c.pages, buf.sink, buf.recent, code,
-                    out, err, stream);
+    return lib.read(lay.l, n, idx, pos, c.seqs, lens, c.table, c.max_pages, c.pool, c.pages, buf.sink, buf.recent,
+                    code | clear, out, err, stream);
   });
 }
 
@@ -377,7 +378,7 @@ PyMethodDef methods[] = {{"bind", method(bind), METH_FASTCALL, nullptr},
                          {"assign", method(entry<assign, 14>), METH_FASTCALL, nullptr},
                          {"norm_rope", method(entry<norm_rope, 9>), METH_FASTCALL, nullptr},
                          {"norm_rope_write", method(entry<norm_rope_write, 16>), METH_FASTCALL, nullptr},
-                         {"read", method(entry<read, 11>), METH_FASTCALL, nullptr},
+                         {"read", method(entry<read, 12>), METH_FASTCALL, nullptr},
                          {"decode_window", method(entry<decode_window, 15>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods};

@@ -31,6 +31,7 @@ struct ReadArgs {
   int32_t* err;
   long long num_pages;
   int n_tokens, num_seqs, max_pages;
+  bool clear;  // the rows of skipped tokens are zeros, not left as they were
 };
 
 constexpr int kWarps = 4;
@@ -127,7 +128,13 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(ReadArgs a) {
 #pragma unroll
     for (int t = 0; t < kRows; ++t) {
       const int kind = kr[t] & 3;
-      if (kind == 0) continue;
+      if (kind == 0) {
+        if (!a.clear || i0 + t0 + t >= a.n_tokens) continue;
+        constexpr int kWords = kDim * (kF32 ? 4 : 2) / 16;
+        uint4* o = static_cast<uint4*>(a.out) + (long long)(i0 + t0 + t) * kWords;
+        for (int c = lane; c < kWords; c += 32) store<kTokens != 1>(o + c, make_uint4(0, 0, 0, 0));
+        continue;
+      }
       float2 f[8], k;
       if (CB == 16 || kind == 1) {
         const uint32_t w[8] = {u0[t].x, u0[t].y, u0[t].z, u0[t].w, u1[t].x, u1[t].y, u1[t].z, u1[t].w};
@@ -230,6 +237,8 @@ extern "C" int mla_lowbit_read(const mla_lowbit_layout* layout, int n_tokens, co
   const int st = check_layout(layout);
   if (st != MLA_LOWBIT_OK) return st;
   if (n_tokens < 0 || num_seqs < 0 || max_pages < 0 || num_pages < 0) return MLA_LOWBIT_ESIZE;
+  const bool clear = (out_dtype & MLA_LOWBIT_CLEAR_SKIPPED) != 0;
+  out_dtype &= ~MLA_LOWBIT_CLEAR_SKIPPED;
   if (out_dtype != MLA_LOWBIT_BF16 && out_dtype != MLA_LOWBIT_FP32) return MLA_LOWBIT_EINVAL;
   if (n_tokens == 0) return MLA_LOWBIT_OK;
   if (num_seqs == 0 || max_pages == 0 || num_pages == 0) return MLA_LOWBIT_ESIZE;
@@ -253,6 +262,7 @@ extern "C" int mla_lowbit_read(const mla_lowbit_layout* layout, int n_tokens, co
   a.n_tokens = n_tokens;
   a.num_seqs = num_seqs;
   a.max_pages = max_pages;
+  a.clear = clear;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int sms = device_sm_count();
   if (sms <= 0) return MLA_LOWBIT_ECUDA;

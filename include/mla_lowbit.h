@@ -94,6 +94,9 @@ enum {
 /* Element types of the calls that take more than one. */
 enum { MLA_LOWBIT_BF16 = 0, MLA_LOWBIT_FP16 = 1, MLA_LOWBIT_FP32 = 2 };
 
+/* OR-ed to mla_lowbit_read's out_dtype: the rows of skipped tokens become zeros. */
+enum { MLA_LOWBIT_CLEAR_SKIPPED = 0x100 };
+
 /* Scaling of the rotation's frequencies for contexts longer than the trained one. */
 enum {
   MLA_LOWBIT_ROPE_NONE = 0,
@@ -403,9 +406,10 @@ int mla_lowbit_norm_rope_write(const mla_lowbit_layout* layout, int n_tokens, co
  * the content groups are rotated back (R, float32).  out is of type out_dtype
  * (MLA_LOWBIT_BF16, to nearest even, or MLA_LOWBIT_FP32), 16-byte aligned.
  * Tokens may come in any order and more than once; seq_idx[i] < 0 is skipped
- * without an error, and the rows of skipped tokens stay as they were.  A
- * sequence index or position out of range (with seq_lens: pos >= seq_lens[s]
- * too) or a bad page sets its error bit. */
+ * without an error.  A sequence index or position out of range (with seq_lens:
+ * pos >= seq_lens[s] too) or a bad page sets its error bit and the token is
+ * skipped.  The rows of skipped tokens stay as they were, or become zeros (out_dtype
+ * | MLA_LOWBIT_CLEAR_SKIPPED). */
 int mla_lowbit_read(const mla_lowbit_layout* layout, int n_tokens, const int32_t* seq_idx,
                     const int32_t* pos, int num_seqs, const int32_t* seq_lens,
                     const int32_t* block_table, int max_pages, const void* page_pool,
