@@ -10,6 +10,7 @@ missing.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -584,12 +585,28 @@ def rope_table(dim: int, theta: float = 10000.0, scaling: str = "none", factor: 
 class Rope:
     """A rotation of ``dim`` channels: frequencies, pair layout and scaling for
     long contexts (``none``, ``linear``, ``ntk`` or ``yarn``), its table on
-    ``device``.  Made once and given to rope, norm_rope and norm_rope_write."""
+    ``device``.  Made once and given to rope, norm_rope and norm_rope_write.
+
+    YaRN sharpens attention over long contexts by t(m) = 0.1 m ln(factor) + 1 on
+    queries and keys.  Where all channels of a head are rotated, all of it is in the
+    rotation (the default: mscale 1, mscale_all_dim 0).  A decoupled key rotates only
+    a part of them, and its checkpoints give both parameters: rotated channels are
+    multiplied by ``self.mscale`` = t(mscale) / t(mscale_all_dim), and the attention's
+    scale by ``self.softmax_factor`` = t(mscale_all_dim)^2, which the caller does."""
 
     def __init__(self, dim: int, theta: float = 10000.0, interleaved: bool = True, scaling: str = "none",
                  factor: float = 1.0, original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
-                 device="cuda"):
+                 device="cuda", mscale: float = 1.0, mscale_all_dim: float = 0.0):
         phase, self.mscale = rope_table(dim, theta, scaling, factor, original_len, beta_fast, beta_slow)
+        self.softmax_factor = 1.0
+        if scaling == "yarn":
+            if not (mscale >= 0 and mscale_all_dim >= 0 and math.isfinite(mscale) and math.isfinite(mscale_all_dim)):
+                raise ValueError(f"mscale and mscale_all_dim must be finite and not below 0, got {mscale}, {mscale_all_dim}")
+            if (mscale, mscale_all_dim) != (1, 0):
+                self.mscale = (0.1 * mscale * math.log(factor) + 1) / (0.1 * mscale_all_dim * math.log(factor) + 1)
+            self.softmax_factor = (0.1 * mscale_all_dim * math.log(factor) + 1) ** 2
+        elif (mscale, mscale_all_dim) != (1, 0):
+            raise ValueError("mscale and mscale_all_dim belong to the scaling 'yarn'")
         self.dim = int(dim)
         self.interleaved = bool(interleaved)
         self.phase = _torch().from_numpy(phase.view(np.int64)).to(device)

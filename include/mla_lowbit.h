@@ -345,7 +345,10 @@ int mla_lowbit_assign(int num_seqs, int max_pages, int num_pages, int max_tokens
  *           max(high - low, 0.001), 0, 1), low = max(floor(c(beta_fast)), 0),
  *           high = min(ceil(c(beta_slow)), rot - 1), c(b) = rot ln(original_len
  *           / (2 pi b)) / (2 ln theta); *mscale = 0.1 ln(factor) + 1.
- * *mscale is 1 for the others.  rot even, 2..2048; theta > 1; factor >= 1;
+ * *mscale is 1 for the others.  (YaRN's factor for heads that are rotated whole.
+ * Checkpoints whose key is rotated in a part give mscale and mscale_all_dim: with
+ * t(m) = 0.1 m ln(factor) + 1 the calls' mscale is t(mscale) / t(mscale_all_dim),
+ * and softmax_scale is multiplied by t(mscale_all_dim)^2.)  rot even, 2..2048; theta > 1; factor >= 1;
  * YARN: original_len >= 1, beta_fast >= beta_slow > 0. */
 int mla_lowbit_rope_table(int rot, double theta, int scaling, double factor, int original_len,
                           double beta_fast, double beta_slow, uint64_t* phase_host,
