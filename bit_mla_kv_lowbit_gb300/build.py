@@ -88,7 +88,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = sources() + [h for d, e in ((CSRC, "cuh"), (CSRC, "h"), (INCLUDE, "h")) for h in glob.glob(os.path.join(d, f"*.{e}"))]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
 

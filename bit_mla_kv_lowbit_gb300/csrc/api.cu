@@ -5,9 +5,9 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
 #include "decode_common.cuh"
+#include "smem_limit.h"
 
 namespace mlalb {
 
@@ -55,21 +55,13 @@ int device_sm_count() {
 }
 
 cudaError_t ensure_smem_limit(const void* kernel, int bytes) {
-  // (device, kernel, bytes) triples already applied; a handful of kernels per device
-  struct Entry { int dev; const void* kernel; int bytes; };
-  static Entry done[256];
-  static int n_done = 0;
-  static std::mutex mu;
+  static SmemLimits limits;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < n_done; ++i)
-    if (done[i].dev == dev && done[i].kernel == kernel && done[i].bytes >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  if (n_done < 256) done[n_done++] = Entry{dev, kernel, bytes};
-  return cudaSuccess;
+  return static_cast<cudaError_t>(limits.ensure(dev, kernel, bytes, [&](int n) {
+    return static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n));
+  }));
 }
 
 }  // namespace mlalb

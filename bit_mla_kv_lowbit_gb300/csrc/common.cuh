@@ -214,9 +214,8 @@ cudaError_t launch_decode_window(int cbits, DecodeArgs a, bool wide, bool out_bf
 int window_ctas_per_split(bool wide, int rows);
 int window_max_split_pages(bool wide);
 cudaError_t launch_decode_wide_window(int cbits, const DecodeArgs& a, cudaStream_t stream);
-// Raises a kernel's dynamic shared-memory limit to `bytes` on the current
-// device, once per (device, kernel): the limit is a per-device attribute.
-// Thread-safe.
+// Raises a kernel's dynamic shared-memory limit on the current device to `bytes`,
+// where it is lower; it is never lowered (smem_limit.h).  Thread-safe.
 cudaError_t ensure_smem_limit(const void* kernel, int bytes);
 // A step is a chain of short kernels, and a launch that waits for the one before
 // to drain costs about as much as some of them.  The kernels of the serving-step

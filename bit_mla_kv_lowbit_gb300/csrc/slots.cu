@@ -347,7 +347,9 @@ extern "C" int mla_lowbit_assign(int num_seqs, int max_pages, int num_pages, int
   const int threads = cluster || release ? kThreads : std::min(kThreads, std::max(256, (want + 31) / 32 * 32));
   auto kern = cluster ? assign_kernel<true> : assign_kernel<false>;
   const int smem = (4 * num_seqs + 3) * (int)sizeof(int);
-  if (ensure_smem_limit(reinterpret_cast<const void*>(kern), smem) != cudaSuccess) return MLA_LOWBIT_ECUDA;
+  constexpr int kNoLimitNeeded = 48 * 1024 - 1024;  // (the kernel's static arrays are below 1 KB)
+  if (smem > kNoLimitNeeded && ensure_smem_limit(reinterpret_cast<const void*>(kern), smem) != cudaSuccess)
+    return MLA_LOWBIT_ECUDA;
   // the second kernel needs the first tokens of the sequences from the first
   a.fill = !(token_start && max_tokens > kFillFrom);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
