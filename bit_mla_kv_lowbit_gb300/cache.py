@@ -34,6 +34,7 @@ class PagedCache:
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         self.device = device
         self._ws = None
+        self._sms = None
         self.seq_lens = None  # the device state of assign: see empty()
 
     @classmethod
@@ -109,8 +110,10 @@ class PagedCache:
             out = binding.new_output((*q.shape[:-1], 512), torch.float32, self.device, stream)
         if workspace is None:
             n = q.shape[1] if q.dim() == 4 else 1
+            if self._sms is None:  # the call plans for the cache's device, whichever is current here
+                self._sms = torch.cuda.get_device_properties(self.pool.device).multi_processor_count
             _, nbytes = binding.window_plan(self.layout, self.num_seqs, q.shape[-2], n, window, sinks,
-                                            self.max_pages)
+                                            self.max_pages, num_sms=self._sms)
             workspace = binding.new_output((nbytes,), torch.uint8, self.device, stream)
         return binding.decode_window(self.layout, q, self.pool, self.block_table, seq_lens, self.sink,
                                      self.recent, out, workspace, self.err, softmax_scale, window,
