@@ -602,7 +602,19 @@ int mla_lowbit_norm_rope(int dtype, int n_tokens, int heads, int dim, const void
                                       : x_token_stride;
     const bool columns = same_strides && d % es == 0 && d / es >= dim && d / es + dim <= inner &&
                          !rows_overlap(n_tokens, x_token_stride, heads, x_head_stride, d / es + dim);
-    if (!columns) return MLA_LOWBIT_EINVAL;
+    // or all heads of a token beside the other array's (all tokens of a head): of every
+    // `outer` elements x has the first ex and y others
+    const long long apart = ya > xa ? d / es : -(d / es);
+    auto beside = [&](long long outer, long long ex, long long ey) {
+      if (outer <= 0 || d % es) return false;
+      const long long r = (apart % outer + outer) % outer;
+      return r >= ex && r + ey <= outer;
+    };
+    const bool tokens = n_tokens > 1 && x_token_stride == y_token_stride &&
+                        beside(x_token_stride, (heads - 1) * x_head_stride + dim, (heads - 1) * y_head_stride + dim);
+    const bool by_head = heads > 1 && x_head_stride == y_head_stride &&
+                         beside(x_head_stride, (n_tokens - 1) * x_token_stride + dim, (n_tokens - 1) * y_token_stride + dim);
+    if (!columns && !tokens && !by_head) return MLA_LOWBIT_EINVAL;
   }
   NormRopeArgs a;
   a.x = x;

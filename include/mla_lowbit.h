@@ -366,7 +366,10 @@ int mla_lowbit_rope_table(int rot, double theta, int scaling, double factor, int
  *             pos[i] (any int32) and multiplied by mscale; rot == 0: none.
  * Computed in float32 and rounded once.  y has strides of its own, which must
  * not make its rows overlap; y may be x itself (same pointer and strides), and
- * must not overlap it otherwise, except as other columns of the same rows.
+ * must not overlap it otherwise.  Arrays between whose ends the other one begins are
+ * taken where they show to be apart: with the same strides as other columns of the
+ * rows, with the same token stride as other columns of the tokens (the heads'
+ * strides may differ), with the same head stride as other columns of the heads.
  *   x, y, weight   of type dtype (MLA_LOWBIT_BF16, _FP16, _FP32), aligned to it
  *   phase          [rot / 2] device copy of mla_lowbit_rope_table's
  *   pos            [n_tokens] int32
