@@ -1065,7 +1065,9 @@ __global__ void __launch_bounds__(kWinCombineWarps * 32) window_combine_kernel(W
     float x[4] = {acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv};
     store_output(orow + 128 * (part * kQuads + k) + 4 * lane, x, a.rotate);
   }
-  if (a.lse && part == 0 && lane == 0) a.lse[row] = lse_of(M, den);
+  // (a split whose sum is not a number has no weight above, but its channels are none
+  // either: so is the logarithm)
+  if (a.lse && part == 0 && lane == 0) a.lse[row] = isnan(acc[0].x) ? acc[0].x : lse_of(M, den);
 }
 
 // Launch the combine as a programmatic dependent of the kernel just queued on

@@ -221,7 +221,7 @@ __device__ __forceinline__ SplitWork window_work(int L, int split, const WinCut&
 }
 // The result of a sequence that is one split (DecodeArgs.win_out).
 __device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  return l <= 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;  // (of a NaN: NaN)
 }
 __device__ __forceinline__ void store_result(const DecodeArgs& a, long long at, float4 v) {
   if (a.win_bf16) {

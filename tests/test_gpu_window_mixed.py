@@ -86,3 +86,30 @@ def test_values_that_are_not_finite_reach_only_who_sees_them(case, one_split):
                     row(s, p).copy_(v)
     assert torch.equal(c.decode_window(q, c.seq_lens, 0.07, W, sinks=K), clean)
     assert c.error() == 0
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("one_split", [False, True])
+def test_lse_of_who_sees_a_nan(case, one_split):
+    # not a number, as the sum that it is the logarithm of; the others' stays
+    import torch
+    import bit_mla_kv_lowbit_gb300 as pkg
+    cb, H, n, W, K, clusters = CASES[case]
+    torch.manual_seed(850 + case)
+    lens = [n, 20, 131, 300, 517]
+    B = len(lens) + (300 if one_split else 40 if clusters else 0)
+    c = pkg.PagedCache.empty(cb, 4 if cb != 16 else 16, B, 9, 9 * len(lens), sum(lens))
+    c.assign(torch.tensor(lens + [0] * (B - len(lens)), dtype=torch.int32, device="cuda"))
+    c.append(torch.randn(sum(lens), 576, device="cuda").bfloat16(), None, pkg.Rope(64))
+    q = torch.randn(B, n, H, 576, device="cuda").bfloat16()
+    lse = [torch.zeros(B, n, H, device="cuda") for _ in range(2)]
+    c.decode_window(q, c.seq_lens, 0.07, W, sinks=K, lse=lse[0])
+    for s, L in enumerate(lens):
+        if cb == 16:
+            c.pool[int(c.block_table[s, (L - 1) // 64])].view(torch.bfloat16).view(64, 576)[(L - 1) % 64, 5] = float("nan")
+        else:
+            (c.sink[s, L - 1] if L <= 4 else c.recent[s, (L - 1) % 128])[5] = float("nan")
+    c.decode_window(q, c.seq_lens, 0.07, W, sinks=K, lse=lse[1])
+    assert bool(torch.isnan(lse[1][:len(lens), n - 1]).all())
+    assert torch.equal(lse[1][:, :n - 1], lse[0][:, :n - 1]) and torch.equal(lse[1][len(lens):], lse[0][len(lens):])
+    assert bool(torch.isneginf(lse[0][len(lens):]).all()) and not bool(torch.isnan(lse[0]).any())
