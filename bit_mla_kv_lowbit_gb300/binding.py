@@ -69,18 +69,24 @@ _INT32_MAX = 2 ** 31 - 1
 _ESIZE = -4
 
 
+def _whole(v, name: str) -> int:
+    if v != int(v):
+        raise ValueError(f"{name} must be a whole number, got {v}")
+    return int(v)
+
+
 def _int32(v, name: str) -> int:
-    v = int(v)
+    v = _whole(v, name)
     if not -_INT32_MAX - 1 <= v <= _INT32_MAX:
         raise ValueError(f"{name} must fit in 32 bits, got {v}")
     return v
 
 
-def _tokens(v) -> int:
+def _tokens(v, name: str) -> int:
     """A window or a number of first tokens: they may exceed every sequence, and
     no sequence is longer than an int32, so what is beyond that is all tokens (and
     below 0 out of range)."""
-    return min(max(int(v), -1), _INT32_MAX)
+    return min(max(_whole(v, name), -1), _INT32_MAX)
 
 
 def _check_sizes(what: str, *sizes: int):
@@ -639,8 +645,8 @@ def _norm_rope(x, pos, rope, offset, norm, weight, eps, out, stream):
         w, p, phase = _pointers(index, ((weight, "weight", dtype, [(dim,)]), (pos, "pos", torch.int32, (n,)),
                                         (rope.phase, "the rope's table", torch.int64, (rot // 2,))))
     _launch(load().mla_lowbit_norm_rope, "mla_lowbit_norm_rope", index,
-            (code, n, heads, dim, x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, norm, w, eps, rot, int(offset), inter, phase,
-             mscale, p), stream)
+            (code, n, heads, dim, x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, norm, w, eps, rot, _whole(offset, "offset"),
+             inter, phase, mscale, p), stream)
     return out
 
 
@@ -755,7 +761,7 @@ def window_plan(lay: Layout, num_seqs: int, heads: int, queries: int, window: in
     splits, nbytes = ctypes.c_int(), ctypes.c_size_t()
     _check(load().mla_lowbit_window_plan(
         ctypes.byref(lay), _int32(num_seqs, "num_seqs"), _int32(heads, "heads"), _int32(queries, "queries"),
-        _tokens(window), _tokens(sinks), _int32(max_pages, "max_pages"), _int32(num_sms, "num_sms"),
+        _tokens(window, "window"), _tokens(sinks, "sinks"), _int32(max_pages, "max_pages"), _int32(num_sms, "num_sms"),
         ctypes.byref(splits), ctypes.byref(nbytes)), "mla_lowbit_window_plan")
     return splits.value, nbytes.value
 
@@ -788,8 +794,9 @@ def decode_window(lay: Layout, q, page_pool, block_table, seq_lens, sink_buf, re
         (out, "out", out.dtype, lead + (512,)), (lse, "lse", f32, [lead]), (workspace, "workspace", u8, None),
         (err_word, "err_word", i32, (1,))))
     _launch(load().mla_lowbit_decode_window, "mla_lowbit_decode_window", index,
-            (ctypes.byref(lay), S, lead[1] if len(lead) == 3 else 1, lead[-1], softmax_scale, _tokens(window), _tokens(sinks), qp,
-             pool, num_pages, table, max_pages, lens, sink, recent, code, o, ls, ws, workspace.numel(), err), stream)
+            (ctypes.byref(lay), S, lead[1] if len(lead) == 3 else 1, lead[-1], softmax_scale, _tokens(window, "window"),
+             _tokens(sinks, "sinks"), qp, pool, num_pages, table, max_pages, lens, sink, recent, code, o, ls, ws,
+             workspace.numel(), err), stream)
     return out
 
 

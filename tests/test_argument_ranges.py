@@ -49,6 +49,18 @@ def test_numbers_that_do_not_fit_are_refused():
         pkg.set_fault_injection(0, -(1 << 64) + 5)
 
 
+def test_parts_of_numbers_are_not_cut_off():
+    lay = pkg.layout(4, 4)
+    plan = dict(num_seqs=2, heads=16, queries=1, window=64, sinks=0, max_pages=8, num_sms=152)
+    for name in plan:
+        with pytest.raises(ValueError, match=name):
+            pkg.window_plan(lay, **{**plan, name: plan[name] + 0.5})
+        assert pkg.window_plan(lay, **{**plan, name: float(plan[name])}) == pkg.window_plan(lay, **plan)
+    for v in (64.5, float("nan")):
+        with pytest.raises(ValueError):
+            pkg.rope_table(v)
+
+
 def test_sizes_of_a_call_are_not_cut():
     # the Python way to a launch: nothing is called when a size does not fit
     b = pkg.binding
@@ -91,6 +103,11 @@ def test_calls_with_numbers_beyond_32_bits(native, monkeypatch):
     for offset in (1 << 32, -(1 << 32), 1 << 40):
         with pytest.raises(pkg.LibraryError):
             pkg.rope(x, pos, pkg.Rope(64), offset=offset)
+    with pytest.raises(ValueError, match="offset"):
+        pkg.rope(x, pos, pkg.Rope(64), offset=2.5)
+    for kw in (dict(window=7.5), dict(window=7, sinks=0.5)):
+        with pytest.raises(ValueError, match="whole"):
+            c.decode_window(q, c.seq_lens, 0.07, **kw)
     # more rows than an int counts, all of them one element
     rows = torch.zeros(1, 1, 1, dtype=torch.bfloat16, device="cuda").expand((1 << 32) + 5, 1, 1)
     with pytest.raises(pkg.LibraryError):
