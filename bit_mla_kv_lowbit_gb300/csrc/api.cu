@@ -332,9 +332,13 @@ int mla_lowbit_decode_multi(const mla_lowbit_layout* layout, int num_seqs, int q
 // which of the two kernels runs it, and how sequences are cut.  Either kernel
 // takes a wave of `fixed` + `unit` ns a unit of its longest split (set-up and
 // epilogue; a page, or a tile of protected tokens), a split's partial costs a write
-// and a read, and the combine of more than one split 3 us.  Measured at 1 to 40 sequences of 32 to 512 rows and windows
-// of 16 to 4,096 tokens, packed and bf16 pages: the estimate is within a tenth of
-// most times, and of the two kernels the other one is at most a tenth faster.
+// and a read, and the combine of more than one split 3 us.  The constants are fits to
+// times of one card at 1 to 40 sequences of 32 to 512 rows, windows of 16 to 4,096
+// tokens and all three layouts, either kernel forced: of those 420 shapes the estimate
+// is within a tenth of the time for 282 and between 0.78 and 1.31 of it for all, and
+// the kernel that it takes is the slower one by more than 5 % for 10 and by more than a
+// tenth for 5, at worst 25.6 against 31.5 us (13 sequences, 3 queries of 32 heads, 512
+// tokens, packed).
 struct WindowPlan {
   WinCut cut;
   bool wide;

@@ -11,19 +11,24 @@
 // arithmetic decides nearly all of them: it gives a value and a bound on its
 // error, and where both ends of that interval round to the same bf16 value, that
 // is the one.  A token with a value for which they do not (about one in six) is
-// redone in two-float arithmetic, to 2^-36 and better.  In the same way a quotient
-// within 1e-5 of a border between two codes is redone by true division.
+// redone in two-float arithmetic, to 2^-36 and better.  In the same way two products,
+// 2^-20 to either side, enclose a code's quotient, and where they round to different
+// codes it is redone by true division.
 //
 // A warp takes a token: lane l holds content channels 16l .. 16l + 15 (a quarter
 // of a group, so a group's minimum is two shuffles and a token's codes are one
 // coalesced store) and one pair of the key.  Large calls run as many warps as
 // fit, each loading its next token while it works on one.
 //
-// 30,011 tokens into INT4 pages, with both bf16 outputs: 29 us (82 MB: 43 % of the
-// measured copy rate; on bf16 pages, without the quantiser, 22 us).  About 640
-// warp instructions a token are the bound (issue slots two thirds busy): 150 the
-// codes, 140 the norm, 70 the rotation, 40 the share of tokens whose norm is
-// redone.  All tokens in two-float arithmetic and by true division took 39 us.
+// 30,011 tokens in a graph, in brackets what their bytes take at the measured copy
+// rate, without and with both bf16 outputs: INT4 pages 27.6 us (6.9) and 28.4 (12.0),
+// rotated 33.1 and 34.0, INT2 29.0 (6.3) and 29.8, rotated 34.2 and 35.5, bf16 pages,
+// without the quantiser, 18.1 (10.4) and 21.2 (15.6).  It is bound by instructions and
+// latency together: about 640 warp instructions a token (150 the codes, 140 the norm,
+// 70 the rotation, 40 the share of tokens whose norm is redone) keep the issue slots
+// 65 % busy with 28 % of the warps that an SM can hold, each in a token's chain of
+// about 25 dependent rounds of shuffles.  All tokens in two-float arithmetic and by
+// true division took 39 us.
 #include <algorithm>
 #include <cmath>
 

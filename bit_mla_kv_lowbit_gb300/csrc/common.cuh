@@ -224,9 +224,11 @@ cudaError_t ensure_smem_limit(const void* kernel, int bytes);
 // every one of their threads does, holds them until it has completed and its
 // writes are visible.  (All threads, also those without work: a kernel that could
 // end before the one it follows would let its own successor overtake that one.)
-// None of them lets its successor start before its own blocks end: clusters of the
-// decode kernel that find their places while other blocks still hold SMs are placed
-// worse (32 x 4,096-token windows at 128 heads: 145 us instead of 136).
+// Only the split kernels of the decode let their successor start before their own
+// blocks end, and that behind their last store, beside the freeing of tensor memory:
+// clusters of the decode kernel that find their places while other blocks still hold
+// SMs for long are placed worse (a trigger at the start of each kernel: 32 x
+// 4,096-token windows at 128 heads 145 us instead of 136).
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... Args>

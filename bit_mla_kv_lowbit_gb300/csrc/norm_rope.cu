@@ -404,7 +404,11 @@ __global__ void __launch_bounds__(kThreads, K == 4 && sizeof(T) == 2 ? (kPart ==
 }
 
 // Rows too long for the registers of a warp: a warp a row, element by element, its
-// floats in shared memory.
+// floats in shared memory.  Norm of rows of 1,536 channels (in brackets what their
+// bytes take at the measured copy rate): bf16 1 row 3.8 us, 128 4.0, 8,192 17.4 (7.5),
+// 65,536 104 (60); float32 3.7, 4.0, 21.6 (15.1) and 140 (121).  It is bound by the
+// element-wise loads, stores and passes through shared memory: 65,536 rows of 1,024
+// bf16 channels, in registers, take 43.6 us (40.2).
 constexpr int kLongWarps = 4;
 template <typename T, bool kNorm>
 __global__ void __launch_bounds__(kLongWarps * 32) norm_rope_long_kernel(NormRopeArgs a) {
