@@ -540,7 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_split_kernel(DecodeArgs a)
         // protected tokens: tile (bf_begin + tile_i - n_pages) of the bf16 list
         const int bt = sw.bf_begin + tile_i - n_pages;
         const int i = bt * kPageTokens + rowB;
-        if (i < sw.n_tok && (!kWin || sees(bf16_pos(sw, i)))) {
+        // the protected-token list is in position order: the masked tokens are
+        // its last n_masked entries (not read: a weight of 0 does not undo a NaN)
+        const int visible = sw.n_tok - n_masked;
+        if (kWin ? i < sw.n_tok && sees(bf16_pos(sw, i)) : i < visible) {
           const int pos = bf16_pos(sw, i);
           if (a.new_ckv && pos == L - 1) {
             rowptr = kRot ? reinterpret_cast<const uint16_t*>(new_rot)
@@ -551,9 +554,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_split_kernel(DecodeArgs a)
                                  : a.recent + ((long long)b * kLocal + pos % kLocal) * kDim;
           }
         }
-        // the protected-token list is in position order: the masked tokens are
-        // its last n_masked entries
-        const int visible = sw.n_tok - n_masked;
         v0 = bt * kPageTokens + tC0 < visible;
         v1 = bt * kPageTokens + tC0 + 1 < visible;
         if constexpr (kWin) {  // (masked rows were not read: their values are 0)
@@ -567,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_split_kernel(DecodeArgs a)
         const bool page_ok = page >= 0 && page < a.num_pages;
         if (!page_ok && ttid == 0) set_error(a.err, MLA_LOWBIT_DEV_BAD_PAGE);
         const int tok0 = page_idx * kPageTokens;
-        if (page_ok && (!kWin || sees(tok0 + rowB)))
+        // (rows behind the end may hold what an earlier sequence left in the page)
+        if (page_ok && (kWin ? sees(tok0 + rowB) : tok0 + rowB < L - n_masked))
           rowptr = reinterpret_cast<const uint16_t*>(a.pool + page * G.page_bytes) + rowB * kDim;
         v0 = page_ok && tok0 + tC0 < L - n_masked;
         v1 = page_ok && tok0 + tC0 + 1 < L - n_masked;

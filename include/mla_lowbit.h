@@ -241,8 +241,8 @@ int mla_lowbit_write_decode(const mla_lowbit_layout* layout, int num_seqs, int h
  * 0 .. L - n + i.  Same arithmetic, tolerance and errors as mla_lowbit_decode
  * otherwise; the n queries run as n blocks of `heads` rows over one pass of the
  * cache (the masked tokens are all inside the recent window, 1 <= n <= 16).
- * On the 128-row kernel a value of these n tokens that is not finite reaches all
- * queries that share its 128 rows, also those before it.
+ * On the 128-row kernel (n * heads a multiple of 128) a value of these n tokens that
+ * is not finite reaches the queries before it too.
  *
  *   q      [num_seqs][n][heads][576] bf16
  *   out    [num_seqs][n][heads][512] float32; lse [num_seqs][n][heads] or NULL
