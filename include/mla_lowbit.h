@@ -183,7 +183,8 @@ int mla_lowbit_decode_plan(const mla_lowbit_layout* layout, int num_seqs, int he
  *   lse[s][h]    = log(sum_t exp(z_t)) (natural log; -inf and out = 0 when L = 0).
  * heads must be a multiple of 16, at most 128 (mla_lowbit_decode_plan takes
  * the rows of a sequence: heads, or n * heads for mla_lowbit_decode_multi,
- * at most 2048).
+ * at most 2048).  On packed layouts queries and protected values take part as
+ * fp16: magnitudes from 65,536 on are infinite there, and what is below 2^-24 is lost.
  *
  *   q             [num_seqs][heads][576] bf16
  *   page_pool     [num_pages][page_bytes] u8 (as written by mla_lowbit_write)
